@@ -27,6 +27,17 @@ constexpr float kBias = 7.0f, kLag = 8.0f;
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float finite_or_zero(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 
+// From a row's products to its scores in units of log 2, where q was scaled by
+// 2^sh = 1 / (i1 i2) and e is the biased exponent of its largest magnitude (255:
+// an infinity or NaN among its values).  Not below the smallest normal number:
+// the product may round to zero for tiny rows or scales, and a masked score is
+// -inf, whose product with zero is NaN.  Products stay below 2^35, so scores that
+// the bound raises stay below 2^-91, which no weight shows.
+__device__ __forceinline__ float score_factor(int e, float scale, float k_gscale, float i1, float i2) {
+  const float f = (scale * i1) * (k_gscale * i2) * kLog2e;
+  return e == 255 ? __builtin_nanf("") : f < 0x1p-126f ? 0x1p-126f : f;
+}
+
 // Sequence of query token t: the last b with starts[b] <= t.
 __device__ __forceinline__ int sequence_of(const KvAttention& a, int t) {
   if (!a.q_starts) return t;
@@ -466,7 +477,7 @@ __global__ __launch_bounds__(256, (Stream<D, kTiles>::kOccupancy)) void kv_atten
           }
         const float i1 = __uint_as_float((uint32_t)(127 - sh / 2) << 23);
         const float i2 = __uint_as_float((uint32_t)(127 - (sh - sh / 2)) << 23);
-        factor[m] = e == 255 ? __builtin_nanf("") : a.scale * k_gscale * kLog2e * i1 * i2;
+        factor[m] = score_factor(e, a.scale, k_gscale, i1, i2);
       }
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) limit_min = min(limit_min, __shfl_xor(limit_min, o, 64));
@@ -815,7 +826,7 @@ __global__ __launch_bounds__(Tile<D>::kThreads, Tile<D>::kOccupancy) void kv_att
       }
     const float i1 = __uint_as_float((uint32_t)(127 - sh / 2) << 23);
     const float i2 = __uint_as_float((uint32_t)(127 - (sh - sh / 2)) << 23);
-    factor = e == 255 ? __builtin_nanf("") : a.scale * k_gscale * kLog2e * i1 * i2;
+    factor = score_factor(e, a.scale, k_gscale, i1, i2);
   }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) limit_min = min(limit_min, __shfl_xor(limit_min, o, 64));
