@@ -489,6 +489,10 @@ class KVCache:
     page_size, D/16], v_codes uint8 [pages, heads, page_size/16, D/2, 16],
     v_scales uint8 [pages, heads, page_size/16, D/16, 16]; k_gscale, v_gscale
     fp32 [1].  Slot s is token s % page_size of page s // page_size.
+
+    The attributes are fixed: calls pass a description that holds the tensors'
+    addresses.  Write into the tensors in place (``cache.k_gscale.copy_(g)``),
+    and make a new KVCache for other tensors or another pool.
     """
 
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_gscale", "v_gscale", "num_pages", "page_size",
@@ -505,17 +509,23 @@ class KVCache:
         _need(v_scales, torch.uint8, (pages, heads, ps // 16, d2 // 8, 16), "v_scales")
         _need(k_gscale, torch.float32, (1,), "k_gscale")
         _need(v_gscale, torch.float32, (1,), "v_gscale")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.k_gscale, self.v_gscale = k_gscale, v_gscale
         for t in (k_scales, v_codes, v_scales, k_gscale, v_gscale):
             if t.device != k_codes.device:
                 raise ValueError("the cache's tensors are on different devices")
-        self.num_pages, self.page_size, self.kv_heads, self.head_dim = pages, ps, heads, 2 * d2
-        self.device = k_codes.device
-        self._index = k_codes.get_device()
-        self._struct = _CacheStruct(*(t.data_ptr() for t in (k_codes, k_scales, v_codes, v_scales, k_gscale, v_gscale)),
-                                    pages, ps, heads, 2 * d2)
-        self._ref = ctypes.addressof(self._struct)
+        tensors = (k_codes, k_scales, v_codes, v_scales, k_gscale, v_gscale)
+        struct = _CacheStruct(*(t.data_ptr() for t in tensors), pages, ps, heads, 2 * d2)
+        for name, value in zip(self.__slots__, tensors + (pages, ps, heads, 2 * d2, k_codes.device, k_codes.get_device(),
+                                                          struct, ctypes.addressof(struct))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name} of a KVCache is fixed: write into its tensors in place, or make a new KVCache")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} of a KVCache is fixed")
+
+    def __reduce__(self):                        # copies describe their own tensors
+        return KVCache, (self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.k_gscale, self.v_gscale)
 
 
 def nvfp4_kv_cache(num_pages, page_size, kv_heads, head_dim, k_gscale=1.0, v_gscale=1.0, device="cuda"):

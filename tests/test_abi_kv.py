@@ -1,6 +1,7 @@
 """CPU checks of the cache entry points: every refusal happens on the host.
 
 The addresses are never dereferenced (see test_abi.py)."""
+import copy
 import ctypes
 
 import pytest
@@ -159,3 +160,31 @@ def test_binding_refuses():
         q.nvfp4_qk_norm_rope(torch.zeros((2, 2, 64), dtype=bf), torch.zeros((2, 2, 64), dtype=bf), None, None, None, None)
     with pytest.raises(ValueError):
         q.nvfp4_qk_norm_rope(torch.zeros((2, 64), dtype=bf), torch.zeros((2, 64), dtype=bf), None, None, None, None)
+
+
+def test_cache_is_fixed(monkeypatch):
+    """The description that calls pass holds the addresses and sizes the cache
+    was made with, so none of them can be exchanged under it."""
+    import torch
+    monkeypatch.setattr(q, "_need", lambda *a: None)                  # tensors of the host serve here
+    u8 = torch.uint8
+    parts = dict(k_codes=torch.zeros((2, 3, 32, 64), dtype=u8), k_scales=torch.zeros((2, 3, 32, 8), dtype=u8),
+                 v_codes=torch.zeros((2, 3, 2, 64, 16), dtype=u8), v_scales=torch.zeros((2, 3, 2, 8, 16), dtype=u8),
+                 k_gscale=torch.ones(1), v_gscale=torch.ones(1))
+    c = q.KVCache(*parts.values())
+    for name, t in parts.items():
+        with pytest.raises(AttributeError, match=name):
+            setattr(c, name, t.clone())
+        with pytest.raises(AttributeError, match=name):
+            delattr(c, name)
+        assert getattr(c, name) is t and getattr(c._struct, name) == t.data_ptr()
+    for name, n in (("num_pages", 2), ("page_size", 32), ("kv_heads", 3), ("head_dim", 128)):
+        with pytest.raises(AttributeError, match=name):
+            setattr(c, name, n + 1)
+        assert getattr(c, name) == n == getattr(c._struct, name)
+    with pytest.raises(AttributeError):
+        c.device = "cuda:1"
+    c.k_gscale.fill_(0.5)                                             # in place is how a scale is set
+    assert copy.copy(c).k_codes is c.k_codes
+    d = copy.deepcopy(c)
+    assert d._struct.k_codes == d.k_codes.data_ptr() != c.k_codes.data_ptr() and d.k_gscale.item() == 0.5
