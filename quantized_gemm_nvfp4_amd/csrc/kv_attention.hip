@@ -1219,6 +1219,10 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvCache c, KvAtt
   const bool live = row < a.total_q * a.q_heads;
   const int t = live ? (int)(row / a.q_heads) : 0, h = live ? (int)(row - (int64_t)t * a.q_heads) : 0;
   const int b = sequence_of(a, t), group = a.q_heads / c.heads;
+  // a query past max_q_len of its sequence, or behind the last one, has no segments
+  const int q0 = a.q_starts ? max(0, a.q_starts[b]) : b, q1 = a.q_starts ? a.q_starts[b + 1] : b + 1;
+  const int64_t query = (int64_t)t - q0;
+  const bool taken = live && t >= q0 && t < q1 && query < a.max_q_len;
   // the row's parts: prefix_chunks of the prefix, then its own
   int own = 1;
   int64_t own_at = cut.full_at + row * cut.own_chunks, own_step = 1, first_off = 0;
@@ -1226,9 +1230,8 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvCache c, KvAtt
   if (cut.workers > 0) {
     const Spot spot = spot_of<false>(a, b, [](int) { return 0; });
     const int share = share_of(cut, spot.all * c.heads * cut.own_tiles);
-    const int local = (t - (a.q_starts ? a.q_starts[b] : b)) * group + h % group;
-    // a row past max_q_len has no worker
-    if (local >= 0 && local < (int64_t)a.max_q_len * group) {
+    if (taken) {
+      const int local = (int)query * group + h % group;
       const int s0 = ((h / group) * cut.own_tiles + local / cut.own_rows) * spot.all + spot.before;
       const int first = s0 / share;
       own = (s0 + passes_of(spot.len) - 1) / share - first + 1;
@@ -1240,7 +1243,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvCache c, KvAtt
       }
     }
   }
-  const bool joined = live && (own > 1 || cut.own_chunks > 1 || cut.prefix_chunks > 0);    // else its workgroup wrote the output
+  const bool joined = taken && (own > 1 || cut.own_chunks > 1 || cut.prefix_chunks > 0);    // else its workgroup wrote the output
   const int parts = joined ? cut.prefix_chunks + own : 0;
   auto index = [&](int p) {
     if (p < cut.prefix_chunks) return row * cut.prefix_chunks + p;
