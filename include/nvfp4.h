@@ -522,7 +522,10 @@ nvfp4_status nvfp4_qk_norm_rope_write(const nvfp4_kv_cache* cache, const void* q
  * q: bf16 [total_q, q_heads, head_dim], q_stride values between tokens (a
  * multiple of 8).  out: bf16 [total_q, q_heads, head_dim], contiguous.
  * q_starts: int32 [batch + 1], ascending from 0 to total_q, or NULL for one
- * query a sequence (total_q == batch, max_q_len == 1).  kv_lens: int32
+ * query a sequence (total_q == batch, max_q_len == 1).  max_q_len: an upper
+ * bound of n known to the host (total_q <= batch * max_q_len is checked); it
+ * sizes the launch.  Rows past max_q_len of their sequence or behind
+ * q_starts[batch] are left as they are.  kv_lens: int32
  * [batch], the tokens that are in the cache already, the queries' own among
  * them.  max_kv_len: an upper bound of kv_lens known to the host, at most
  * table_width * page_size; it sizes the launch.  page_table: int32 [batch,

@@ -720,7 +720,7 @@ def _attention_workspace(index, pages, page_size, heads, d, q_heads, batch, tota
                                                         prefix_len)
 
 
-def nvfp4_kv_attention(q, cache, page_table, kv_lens, q_starts=None, max_q_len=1, max_kv_len=None, prefix_pages=None,
+def nvfp4_kv_attention(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None, max_kv_len=None, prefix_pages=None,
                        prefix_len=0, scale=None, out=None, workspace=None):
     """Causal attention of new tokens over the cache: softmax(scale q K^T) V.
 
@@ -728,7 +728,8 @@ def nvfp4_kv_attention(q, cache, page_table, kv_lens, q_starts=None, max_q_len=1
     page_table: int32 [batch, width]; kv_lens: int32 [batch], cached tokens of
     each sequence, its new ones included.  q_starts: int32 [batch + 1], the
     rows of q of each sequence (None: one query a sequence); max_q_len: the
-    most queries of a sequence.  max_kv_len: the host's upper bound of kv_lens
+    host's upper bound of a sequence's queries (default: all T, which always
+    holds; a close one is faster).  max_kv_len: the host's upper bound of kv_lens
     (default: the page table's width).  prefix_pages (int32), prefix_len:
     tokens that every sequence of the batch has in front of its own; they are
     computed once for all.  scale: default D ** -0.5.  Returns bf16
@@ -743,6 +744,8 @@ def nvfp4_kv_attention(q, cache, page_table, kv_lens, q_starts=None, max_q_len=1
     batch, width = page_table.shape
     lens = _data(kv_lens, torch.int32, (batch,), "kv_lens", index)
     starts = _data(q_starts, torch.int32, (batch + 1,), "q_starts", index) if q_starts is not None else None
+    if max_q_len is None:
+        max_q_len = total if starts is not None else 1
     if max_kv_len is None:
         max_kv_len = width * cache.page_size
     prefix = None

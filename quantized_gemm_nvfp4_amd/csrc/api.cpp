@@ -335,6 +335,9 @@ nvfp4_status check_attention(const nvfp4k::KvCache& c, int64_t q_heads, int64_t 
   if (total_q > 0 && (batch < 1 || max_q_len < 1))
     return fail(NVFP4_ERR_INVALID_ARG, "batch=%lld and max_q_len=%lld must be positive with total_q=%lld",
                 (long long)batch, (long long)max_q_len, (long long)total_q);
+  if (total_q > batch * max_q_len)
+    return fail(NVFP4_ERR_INVALID_ARG, "total_q=%lld: q_starts cannot lay them out in batch=%lld sequences of at most max_q_len=%lld",
+                (long long)total_q, (long long)batch, (long long)max_q_len);
   if (total_q * q_heads >= kMaxKvRows)
     return fail(NVFP4_ERR_UNSUPPORTED, "total_q * q_heads exceeds 2^31 rows (total_q=%lld)", (long long)total_q);
   // key positions and the look-ahead past them stay in int

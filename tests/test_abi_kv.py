@@ -188,3 +188,42 @@ def test_cache_is_fixed(monkeypatch):
     assert copy.copy(c).k_codes is c.k_codes
     d = copy.deepcopy(c)
     assert d._struct.k_codes == d.k_codes.data_ptr() != c.k_codes.data_ptr() and d.k_gscale.item() == 0.5
+
+
+def test_attention_refuses_more_queries_than_max_q_len_allows():
+    """Rows past max_q_len of their sequence would be left as they were."""
+    P_STARTS = P(0x20)
+    assert att(starts=P_STARTS, total=4, mq=1) == INVALID and "max_q_len" in err()
+    assert att(starts=P_STARTS, total=4000, batch=3, mq=1333) == INVALID and "max_q_len" in err()
+    assert att(starts=P_STARTS, total=4000, batch=3, mq=1334, ws=None, wsn=0, mkv=129) == SHAPE      # the next check
+    assert q.lib().nvfp4_kv_attention_workspace_bytes(cache(), 4, 3, 4000, 1333, 100000, 0) == 0
+
+
+@pytest.mark.parametrize("given,want", [({}, 7), (dict(max_q_len=5), 5), (dict(q_starts=None), 1)])
+def test_binding_takes_a_bound_that_always_holds(monkeypatch, given, want):
+    """Without max_q_len, any one sequence may hold every query."""
+    import torch
+    seen = []
+
+    class Lib:
+        def nvfp4_kv_attention_workspace_bytes(self, ref, hq, batch, total, max_q_len, *rest):
+            seen.append(max_q_len)
+            return 0
+
+        def nvfp4_kv_attention(self, ref, qp, qs, hq, starts, batch, total, max_q_len, *rest):
+            seen.append(max_q_len)
+            return 0
+
+    class Cache:
+        _index, head_dim, page_size, num_pages, kv_heads, _ref, device = -1, 64, 16, 4, 2, 0, "cpu"
+
+    monkeypatch.setattr(q, "lib", Lib)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
+    monkeypatch.setattr(q, "_attention_workspace", lambda *a: Lib().nvfp4_kv_attention_workspace_bytes(0, *a[5:]))
+    batch = 7 if "q_starts" in given else 3
+    args = dict(q_starts=torch.tensor([0, 0, 7, 7], dtype=torch.int32))
+    args.update(given)
+    q.nvfp4_kv_attention(torch.zeros((7, 4, 64), dtype=torch.bfloat16), Cache, torch.zeros((batch, 2), dtype=torch.int32),
+                         torch.zeros(batch, dtype=torch.int32), **args)
+    assert seen == [want, want]
