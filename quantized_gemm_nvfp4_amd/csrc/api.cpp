@@ -346,7 +346,9 @@ nvfp4_status check_attention(const nvfp4k::KvCache& c, int64_t q_heads, int64_t 
   a->batch = (int32_t)batch;
   a->total_q = total_q;
   a->q_heads = (int32_t)q_heads;
-  a->max_q_len = (int32_t)max_q_len;
+  // no sequence has more queries than there are rows: with that the row tiles
+  // of a sequence stay in int, as total_q * q_heads does
+  a->max_q_len = (int32_t)(max_q_len < total_q ? max_q_len : total_q);
   a->max_kv_len = (int32_t)max_kv_len;
   a->prefix_len = (int32_t)prefix_len;
   if (total_q > 0 && !nvfp4k::kv_attention_supported(c, *a))

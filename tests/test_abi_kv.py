@@ -227,3 +227,19 @@ def test_binding_takes_a_bound_that_always_holds(monkeypatch, given, want):
     q.nvfp4_kv_attention(torch.zeros((7, 4, 64), dtype=torch.bfloat16), Cache, torch.zeros((batch, 2), dtype=torch.int32),
                          torch.zeros(batch, dtype=torch.int32), **args)
     assert seen == [want, want]
+
+
+def test_attention_bound_far_past_the_queries():
+    """No sequence has more queries than there are rows: a larger max_q_len
+    asks for no more than total_q does (its row tiles would not fit an int)."""
+    def f(mq, hq=4, heads=2, total=300, **kw):
+        a = dict(mkv=100000, plen=0)
+        a.update(kw)
+        return q.lib().nvfp4_kv_attention_workspace_bytes(cache(heads=heads), hq, 3, total, mq, a["mkv"], a["plen"])
+    for kw in ({}, dict(hq=128), dict(plen=5000), dict(hq=128, heads=1, plen=70), dict(total=3)):
+        want = f(kw.get("total", 300), **kw)
+        assert want > 0
+        for mq in (301, 5000, (1 << 31) - 1):
+            assert f(mq, **kw) == want, (kw, mq)
+    big = dict(width=1 << 20, mkv=100000, starts=P(0x20), total=300, mq=(1 << 31) - 1)
+    assert att(ws=None, wsn=0, **big) == INVALID and "workspace" in err()
