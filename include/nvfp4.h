@@ -435,7 +435,8 @@ nvfp4_status nvfp4_gemm_lora_ex(const uint8_t* a_codes, const uint8_t* a_scales,
  * Device-side indices are checked in the kernels, since the host never reads
  * them: a slot outside [0, num_pages * page_size) is padding, a page number
  * outside [0, num_pages) hides its tokens, a length is taken within
- * [0, max_kv_len].
+ * [0, max_kv_len].  Calls of no tokens do nothing; their rows, slots, lengths
+ * and page tables may be NULL.
  */
 typedef struct nvfp4_kv_cache {
   uint8_t* k_codes;

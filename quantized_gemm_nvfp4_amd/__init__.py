@@ -652,8 +652,10 @@ def _norm_rope_args(q, k, q_weight, k_weight, cos_sin, positions):
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_pos, rot_dim]")
     max_pos, rot = cos_sin.shape
-    return (index, d, tokens, hq, qs, hk, ks, qw, kw, cp, max_pos, rot,
-            _data(positions, torch.int32, (tokens,), "positions", index))
+    # an empty tensor's address is null, which the library takes for a missing
+    # argument; it reads no position of no tokens
+    pp = _data(positions, torch.int32, (tokens,), "positions", index) or cp
+    return index, d, tokens, hq, qs, hk, ks, qw, kw, cp, max_pos, rot, pp
 
 
 def nvfp4_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interleaved=False, out=None):

@@ -271,9 +271,10 @@ void cache_ranges(const nvfp4_kv_cache& c, Range* r) {
   r[5] = {c.v_gscale, 4, "v_gscale"};
 }
 
-// A strided bf16 operand of `tokens` rows of `width` values.
+// A strided bf16 operand of `tokens` rows of `width` values; with no rows it
+// may be null (an empty tensor's address).
 nvfp4_status check_rows(const void* p, const char* name, int64_t stride, int64_t width, int64_t tokens) {
-  if (p == nullptr) return fail(NVFP4_ERR_INVALID_ARG, "%s is a null pointer", name);
+  if (p == nullptr && tokens > 0) return fail(NVFP4_ERR_INVALID_ARG, "%s is a null pointer", name);
   if (!aligned(p, 16)) return fail(NVFP4_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
   if (stride < width) return fail(NVFP4_ERR_SHAPE, "%s has token stride %lld below its row of %lld", name,
                                   (long long)stride, (long long)width);
@@ -848,7 +849,7 @@ nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k_bf16, int
   const int64_t width = cache->kv_heads * cache->head_dim;
   if (nvfp4_status s = check_rows(k_bf16, "k", k_stride, width, tokens)) return s;
   if (nvfp4_status s = check_rows(v_bf16, "v", v_stride, width, tokens)) return s;
-  REQUIRE_PTR(slots);
+  if (tokens > 0) REQUIRE_PTR(slots);
   REQUIRE_ALIGN(slots, 8);
   if (tokens * 2 * cache->kv_heads >= kMaxKvRows)
     return fail(NVFP4_ERR_UNSUPPORTED, "tokens * heads exceeds 2^31 rows (tokens=%lld)", (long long)tokens);
@@ -871,7 +872,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, in
   const int64_t width = cache->kv_heads * cache->head_dim;
   if (nvfp4_status s = check_rows(k_bf16, "k", width, width, tokens)) return s;
   if (nvfp4_status s = check_rows(v_bf16, "v", width, width, tokens)) return s;
-  REQUIRE_PTR(slots);
+  if (tokens > 0) REQUIRE_PTR(slots);
   REQUIRE_ALIGN(slots, 8);
   if (tokens * 2 * cache->kv_heads >= kMaxKvRows)
     return fail(NVFP4_ERR_UNSUPPORTED, "tokens * heads exceeds 2^31 rows (tokens=%lld)", (long long)tokens);
@@ -938,7 +939,7 @@ nvfp4_status nvfp4_qk_norm_rope_write(const nvfp4_kv_cache* cache, const void* q
   if (nvfp4_status s = check_rows(k_bf16, "k", k_stride, kw, tokens)) return s;
   if (nvfp4_status s = check_rows(v_bf16, "v", v_stride, kw, tokens)) return s;
   if (nvfp4_status s = check_rows(q_out_bf16, "q_out", q_out_stride, qw, tokens)) return s;
-  REQUIRE_PTR(slots);
+  if (tokens > 0) REQUIRE_PTR(slots);
   REQUIRE_ALIGN(slots, 8);
   if (tokens == 0) return ok();
   if (nvfp4_status s = check_rows_disjoint(q_out_bf16, "q_out", q_out_stride, qw, q_bf16, "q", q_stride, qw, tokens, true)) return s;
@@ -984,8 +985,11 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q_bf16,
   if (nvfp4_status s = check_attention(c, q_heads, batch, total_q, max_q_len, max_kv_len, prefix_len, &a)) return s;
   const int64_t width = q_heads * cache->head_dim;
   if (nvfp4_status s = check_rows(q_bf16, "q", q_stride, width, total_q)) return s;
-  REQUIRE_PTR(kv_lens);
-  REQUIRE_PTR(out_bf16);
+  if (total_q > 0) {
+    REQUIRE_PTR(kv_lens);
+    REQUIRE_PTR(out_bf16);
+    if (max_kv_len > 0) REQUIRE_PTR(page_table);
+  }
   REQUIRE_ALIGN(kv_lens, 4);
   REQUIRE_ALIGN(out_bf16, 16);
   if (table_width < 0 || table_width > kMaxDim)
@@ -993,7 +997,6 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, const void* q_bf16,
   if (max_kv_len > table_width * cache->page_size)
     return fail(NVFP4_ERR_SHAPE, "max_kv_len=%lld exceeds the page table's %lld pages of %lld tokens",
                 (long long)max_kv_len, (long long)table_width, (long long)cache->page_size);
-  if (max_kv_len > 0) REQUIRE_PTR(page_table);
   REQUIRE_ALIGN(page_table, 4);
   if (prefix_len > 0) REQUIRE_PTR(prefix_pages);
   REQUIRE_ALIGN(prefix_pages, 4);

@@ -243,3 +243,18 @@ def test_attention_bound_far_past_the_queries():
             assert f(mq, **kw) == want, (kw, mq)
     big = dict(width=1 << 20, mkv=100000, starts=P(0x20), total=300, mq=(1 << 31) - 1)
     assert att(ws=None, wsn=0, **big) == INVALID and "workspace" in err()
+
+
+def test_no_tokens_need_no_pointers():
+    """An empty tensor's address is null: calls of no tokens do nothing."""
+    assert write(k=None, v=None, slots=None, tokens=0) == OK
+    assert read(slots=None, k=None, v=None, tokens=0) == OK
+    assert norm(qp=None, qo=None, kp=None, ko=None, tokens=0) == OK
+    lib = q.lib()
+    assert lib.nvfp4_qk_norm_rope_write(cache(heads=1), None, 256, None, None, 256, 2, None, 128, None, None, 128, T, 9, 128,
+                                        0, SL, 1e-6, None, 0, None) == OK
+    assert att(qp=None, out=None, table=None, lens=None, batch=0, total=0) == OK
+    assert att(qp=None, out=None, starts=P(0x20), total=0) == OK
+    # what else is wrong with them is still said
+    assert write(k=None, v=None, slots=None, ks=248, tokens=0) == SHAPE
+    assert norm(qp=None, qo=None, kp=None, ko=None, rot=12) == SHAPE

@@ -216,3 +216,24 @@ def test_another_stream():
     want, _, _, _ = expect_pages(bits.reshape(64, 2, 128), np.arange(64), 4, 16, 2, 128, KG, False)
     assert np.array_equal(host_u8(cache.k_codes), want)
     assert torch.isfinite(k.float()).all() and torch.isfinite(v.float()).all()
+
+
+def test_no_tokens():
+    """Empty tensors go through every operator."""
+    torch = need_gpu()
+    import quantized_gemm_nvfp4_amd as q
+    log("cache operators on no tokens")
+    cache = make_cache(torch, q, 2, 16, 2, 128)
+    none = torch.empty((0, 2, 128), dtype=torch.bfloat16, device="cuda")
+    i32, i64 = (torch.empty(0, dtype=t, device="cuda") for t in (torch.int32, torch.int64))
+    table = torch.ones((9, 128), device="cuda")
+    q.nvfp4_kv_write(none, none, cache, i64)
+    outs = [*q.nvfp4_kv_read(cache, i64), *q.nvfp4_qk_norm_rope(none, none, None, None, table, i32),
+            q.nvfp4_qk_norm_rope_write(none, none, none, None, None, table, i32, cache, i64),
+            q.nvfp4_kv_attention(none, cache, torch.zeros((0, 3), dtype=torch.int32, device="cuda"), i32),
+            q.nvfp4_kv_attention(none, cache, torch.zeros((2, 3), dtype=torch.int32, device="cuda"),
+                                 torch.zeros(2, dtype=torch.int32, device="cuda"),
+                                 q_starts=torch.zeros(3, dtype=torch.int32, device="cuda"))]
+    torch.cuda.synchronize()
+    assert all(o.shape == (0, 2, 128) for o in outs)
+    assert (host_u8(cache.k_codes) == 0xA5).all() and (host_u8(cache.v_scales) == 0xA5).all()
