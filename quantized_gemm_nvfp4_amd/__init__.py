@@ -559,7 +559,7 @@ def _rows(t, heads, d, name, index):
             n, h, w = t.shape
             s0, s1, s2 = t.stride()
             if w == d and s2 == 1 and (s1 == d or h == 1) and (heads is None or h == heads):
-                return n, h, s0 if n > 1 else max(s0, h * d)
+                return n, h, s0 if n > 1 else h * d
             if w != d or (heads is not None and h != heads):
                 raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, {heads or 'heads'}, {d}]")
             raise ValueError(f"{name} must have contiguous rows (strides {t.stride()})")

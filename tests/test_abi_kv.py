@@ -258,3 +258,13 @@ def test_no_tokens_need_no_pointers():
     # what else is wrong with them is still said
     assert write(k=None, v=None, slots=None, ks=248, tokens=0) == SHAPE
     assert norm(qp=None, qo=None, kp=None, ko=None, rot=12) == SHAPE
+
+
+def test_stride_of_a_single_token_does_not_matter():
+    """A slice of one row keeps its buffer's pitch, whatever that is."""
+    import torch
+    buf = torch.zeros(2 * 300, dtype=torch.bfloat16)
+    one = torch.as_strided(buf, (1, 2, 128), (300, 128, 1))
+    assert q._rows(one, 2, 128, "k", -1) == (1, 2, 256)
+    assert q._rows(one[:0], 2, 128, "k", -1) == (0, 2, 256)
+    assert q._rows(torch.as_strided(buf, (2, 2, 128), (300, 128, 1)), 2, 128, "k", -1) == (2, 2, 300)

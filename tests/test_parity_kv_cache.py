@@ -237,3 +237,28 @@ def test_no_tokens():
     torch.cuda.synchronize()
     assert all(o.shape == (0, 2, 128) for o in outs)
     assert (host_u8(cache.k_codes) == 0xA5).all() and (host_u8(cache.v_scales) == 0xA5).all()
+
+
+def test_one_token_of_an_odd_pitch():
+    torch = need_gpu()
+    import quantized_gemm_nvfp4_amd as q
+    log("cache operators on one token of a row of 261 values")
+    buf = dev_bf16(workloads.random_bf16(797, (1, 261)))
+    x = torch.as_strided(buf, (1, 2, 128), (261, 128, 1))
+    whole = x.contiguous()
+    st = torch.tensor([5], dtype=torch.int64, device="cuda")
+    a, b = make_cache(torch, q, 1, 16, 2, 128), make_cache(torch, q, 1, 16, 2, 128)
+    q.nvfp4_kv_write(x, x, a, st)
+    q.nvfp4_kv_write(whole, whole, b, st)
+    ya = q.nvfp4_qk_norm_rope(x, x, None, None, None, None)
+    yb = q.nvfp4_qk_norm_rope(whole, whole, None, None, None, None)
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.tensor([6], dtype=torch.int32, device="cuda")
+    oa, ob = (q.nvfp4_kv_attention(t, a, table, lens) for t in (x, whole))
+    torch.cuda.synchronize()
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
+    for u, w in ((ya[0], yb[0]), (ya[1], yb[1]), (oa, ob)):
+        assert torch.equal(u.view(torch.int16), w.view(torch.int16))
+    q.nvfp4_qk_norm_rope(x, x.clone(), None, None, None, None, out=(x, whole))            # in place
+    torch.cuda.synchronize()
+    assert torch.equal(x.contiguous().view(torch.int16), yb[0].view(torch.int16))
