@@ -245,7 +245,7 @@ def test_one_token_of_an_odd_pitch():
     log("cache operators on one token of a row of 261 values")
     buf = dev_bf16(workloads.random_bf16(797, (1, 261)))
     x = torch.as_strided(buf, (1, 2, 128), (261, 128, 1))
-    whole = x.contiguous()
+    whole = x.clone(memory_format=torch.contiguous_format)
     st = torch.tensor([5], dtype=torch.int64, device="cuda")
     a, b = make_cache(torch, q, 1, 16, 2, 128), make_cache(torch, q, 1, 16, 2, 128)
     q.nvfp4_kv_write(x, x, a, st)
