@@ -325,6 +325,12 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// The hardware's reciprocal root takes denormal numbers for zero.
+__device__ __forceinline__ float rsqrt_of(float x) {
+  const bool tiny = x < 0x1p-126f;
+  return __builtin_amdgcn_rsqf(tiny ? x * 0x1p32f : x) * (tiny ? 0x1p16f : 1.0f);
+}
+
 template <int D, int kRows, bool kInter, bool kWrite>
 __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope a, KvCache c, const int64_t* slots,
                                                         const uint16_t* v, int64_t v_stride, int64_t row_groups) {
@@ -403,7 +409,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope a, KvCache c, c
       ss = __builtin_fmaf(y[2 * j], y[2 * j], ss);
       ss = __builtin_fmaf(y[2 * j + 1], y[2 * j + 1], ss);
     }
-    const float r = __builtin_amdgcn_rsqf(row_sum<kLanes>(ss) * (1.0f / D) + a.eps);
+    const float r = rsqrt_of(row_sum<kLanes>(ss) * (1.0f / D) + a.eps);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       y[2 * j] = y[2 * j] * r * __uint_as_float(w[j] << 16);

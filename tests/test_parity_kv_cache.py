@@ -262,3 +262,25 @@ def test_one_token_of_an_odd_pitch():
     q.nvfp4_qk_norm_rope(x, x.clone(), None, None, None, None, out=(x, whole))            # in place
     torch.cuda.synchronize()
     assert torch.equal(x.contiguous().view(torch.int16), yb[0].view(torch.int16))
+
+
+@pytest.mark.parametrize("sigma,eps", [(2.0 ** -64, 0.0), (2.0 ** -64, 1e-42), (2.0 ** -70, 1e-39), (2.0 ** -62, 1e-38)])
+def test_norm_of_rows_whose_squares_are_denormal(sigma, eps):
+    """The mean square is below the smallest normal float; its root is not."""
+    torch = need_gpu()
+    import quantized_gemm_nvfp4_amd as q
+    log(f"norm_rope sigma {sigma} eps {eps}")
+    rng = np.random.default_rng(23)
+    bits = workloads.random_bf16(798, (20, 4 * 128), sigma=sigma)
+    if eps > 0:
+        bits[3, :128] = 0
+    x = dev_bf16(bits).view(20, 4, 128)
+    ang = rng.uniform(-3, 3, (9, 64))
+    table = np.concatenate((np.cos(ang), np.sin(ang)), 1).astype(np.float32)
+    pos = rng.integers(0, 9, 20)
+    eps = float(np.float32(eps))
+    yq, yk = q.nvfp4_qk_norm_rope(x[:, :3], x[:, 3:], None, None, torch.tensor(table, device="cuda"),
+                                  torch.tensor(pos, dtype=torch.int32, device="cuda"), eps=eps)
+    torch.cuda.synchronize()
+    check_norm(host_bits(yq), bits.reshape(20, 4, 128)[:, :3], None, table, pos, eps, 128, False)
+    check_norm(host_bits(yk), bits.reshape(20, 4, 128)[:, 3:], None, table, pos, eps, 128, False)
