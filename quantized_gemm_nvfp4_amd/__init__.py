@@ -134,6 +134,21 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _launch(index, fn, *args):
+    """fn(*args, stream) on the current stream of device `index`, the one the
+    operands are on, with that device current: a stream's handle (0 for the
+    default one) means what it does on the current device, and kernels are
+    launched there."""
+    native = _torch_module._C                        # loaded with the library fn is from
+    if native._cuda_getDevice() == index:
+        status = fn(*args, native._cuda_getCurrentRawStream(index))
+    else:
+        with _torch_module.cuda.device(index):
+            status = fn(*args, native._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status)
+
+
 def _need(t, dtype, shape, name):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
@@ -182,8 +197,8 @@ def nvfp4_quantize(x, global_scale=None, out=None, rule="absmax"):
         ws = torch.empty(lib().nvfp4_quantize_workspace_bytes(), dtype=torch.uint8, device=x.device)
     if rule not in SCALE_RULES:
         raise ValueError(f"unknown scale rule {rule!r}; one of {sorted(SCALE_RULES)}")
-    _check(lib().nvfp4_quantize_ex(_ptr(x), rows, cols, _ptr(codes), _ptr(scales), _ptr(g), use_given,
-                                   SCALE_RULES[rule], _ptr(ws) if ws is not None else None, _stream(x)))
+    _launch(x.get_device(), lib().nvfp4_quantize_ex, _ptr(x), rows, cols, _ptr(codes), _ptr(scales), _ptr(g),
+            use_given, SCALE_RULES[rule], _ptr(ws) if ws is not None else None)
     return codes, scales, g
 
 
@@ -215,9 +230,9 @@ def nvfp4_gemm(a, w, algo=ALGO_AUTO, out=None, workspace=None):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=ac.device)
     if workspace is not None:
         _need(workspace, torch.uint8, None, "workspace")
-    _check(lib().nvfp4_gemm_ws(_ptr(ac), _ptr(as_), _ptr(ag), _ptr(wc), _ptr(ws), _ptr(wg), _ptr(out),
-                               M, N, K, int(algo), _ptr(workspace) if workspace is not None else None,
-                               workspace.numel() if workspace is not None else 0, _stream(ac)))
+    _launch(ac.get_device(), lib().nvfp4_gemm_ws, _ptr(ac), _ptr(as_), _ptr(ag), _ptr(wc), _ptr(ws), _ptr(wg),
+            _ptr(out), M, N, K, int(algo), _ptr(workspace) if workspace is not None else None,
+            workspace.numel() if workspace is not None else 0)
     return out
 
 
@@ -250,9 +265,9 @@ def nvfp4_gemm_amax(a, w, out=None, workspace=None, slots=None):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=ac.device)
     if workspace is not None:
         _need(workspace, torch.uint8, None, "workspace")
-    _check(lib().nvfp4_gemm_amax(_ptr(ac), _ptr(as_), _ptr(ag), _ptr(wc), _ptr(ws), _ptr(wg), _ptr(out), M, N, K,
-                                 _ptr(workspace) if workspace is not None else None,
-                                 workspace.numel() if workspace is not None else 0, _ptr(slots), _stream(ac)))
+    _launch(ac.get_device(), lib().nvfp4_gemm_amax, _ptr(ac), _ptr(as_), _ptr(ag), _ptr(wc), _ptr(ws), _ptr(wg),
+            _ptr(out), M, N, K, _ptr(workspace) if workspace is not None else None,
+            workspace.numel() if workspace is not None else 0, _ptr(slots))
     return out, slots[:nslots]
 
 
@@ -274,8 +289,8 @@ def nvfp4_quantize_amax(x, slots, out=None):
     _need(codes, torch.uint8, (rows, cols // 2), "codes")
     _need(scales, torch.uint8, (rows, cols // 16), "scales")
     _need(g, torch.float32, (1,), "global_scale")
-    _check(lib().nvfp4_quantize_amax(_ptr(x), rows, cols, _ptr(codes), _ptr(scales), _ptr(g), _ptr(slots),
-                                     slots.numel(), _stream(x)))
+    _launch(x.get_device(), lib().nvfp4_quantize_amax, _ptr(x), rows, cols, _ptr(codes), _ptr(scales), _ptr(g),
+            _ptr(slots), slots.numel())
     return codes, scales, g
 
 
@@ -294,7 +309,8 @@ def nvfp4_gemm_w4a16(x, w, algo=ALGO_AUTO, out=None):
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     _need(out, torch.bfloat16, (M, N), "out")
-    _check(lib().nvfp4_gemm_w4a16_ex(_ptr(x), _ptr(wc), _ptr(ws), _ptr(wg), _ptr(out), M, N, K, algo, _stream(x)))
+    _launch(x.get_device(), lib().nvfp4_gemm_w4a16_ex, _ptr(x), _ptr(wc), _ptr(ws), _ptr(wg), _ptr(out), M, N, K,
+            algo)
     return out
 
 
@@ -334,9 +350,9 @@ def nvfp4_linear(x, w, out=None, x_out=None, workspace=None):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     if workspace is not None:
         _need(workspace, torch.uint8, None, "workspace")
-    _check(lib().nvfp4_linear(_ptr(x), _ptr(wc), _ptr(ws), _ptr(wg), _ptr(out), M, N, K, _ptr(xc), _ptr(xs),
-                              _ptr(xg), _ptr(workspace) if workspace is not None else None,
-                              workspace.numel() if workspace is not None else 0, _stream(x)))
+    _launch(x.get_device(), lib().nvfp4_linear, _ptr(x), _ptr(wc), _ptr(ws), _ptr(wg), _ptr(out), M, N, K, _ptr(xc),
+            _ptr(xs), _ptr(xg), _ptr(workspace) if workspace is not None else None,
+            workspace.numel() if workspace is not None else 0)
     return out, x_out
 
 
@@ -367,9 +383,8 @@ def nvfp4_quantize_lora(x, lora_down, global_scale=None, out=None):
     _need(g, torch.float32, (1,), "global_scale")
     _need(t, torch.float32, (rows, r), "t")
     ws = torch.empty(lib().nvfp4_quantize_lora_workspace_bytes(rows, cols, r), dtype=torch.uint8, device=x.device)
-    _check(lib().nvfp4_quantize_lora(_ptr(x), rows, cols, _ptr(codes), _ptr(scales), _ptr(g),
-                                     1 if global_scale is not None else 0, _ptr(lora_down), r, _ptr(t), _ptr(ws),
-                                     _stream(x)))
+    _launch(x.get_device(), lib().nvfp4_quantize_lora, _ptr(x), rows, cols, _ptr(codes), _ptr(scales), _ptr(g),
+            1 if global_scale is not None else 0, _ptr(lora_down), r, _ptr(t), _ptr(ws))
     return codes, scales, g, t
 
 
@@ -395,8 +410,8 @@ def nvfp4_gemm_lora(a, w, t, lora_up, algo=ALGO_AUTO, out=None):
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=ac.device)
     _need(out, torch.bfloat16, (M, N), "out")
-    _check(lib().nvfp4_gemm_lora_ex(_ptr(ac), _ptr(as_), _ptr(ag), _ptr(wc), _ptr(ws), _ptr(wg), _ptr(t),
-                                    _ptr(lora_up), r, _ptr(out), M, N, K, int(algo), _stream(ac)))
+    _launch(ac.get_device(), lib().nvfp4_gemm_lora_ex, _ptr(ac), _ptr(as_), _ptr(ag), _ptr(wc), _ptr(ws), _ptr(wg),
+            _ptr(t), _ptr(lora_up), r, _ptr(out), M, N, K, int(algo))
     return out
 
 
@@ -419,7 +434,7 @@ def int4g_quantize(w, group=128, out=None):
         s = torch.empty((N, K // group if group else 0), dtype=torch.float16, device=w.device)
     else:
         q, s = out
-    _check(lib().int4g_quantize(_ptr(w), N, K, group, _ptr(q), _ptr(s), _stream(w)))
+    _launch(w.get_device(), lib().int4g_quantize, _ptr(w), N, K, group, _ptr(q), _ptr(s))
     return q, s
 
 
@@ -434,8 +449,7 @@ def int4g_gemv(x, q, scales, group=128, algo=ALGO_AUTO, out=None):
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     _need(out, torch.bfloat16, (M, N), "out")
-    _check(lib().int4g_gemv_ex(_ptr(x), _ptr(q), _ptr(scales), _ptr(out), M, N, K, group, int(algo),
-                               _stream(x)))
+    _launch(x.get_device(), lib().int4g_gemv_ex, _ptr(x), _ptr(q), _ptr(scales), _ptr(out), M, N, K, group, int(algo))
     return out
 
 
@@ -455,7 +469,7 @@ def int4g_asym_quantize(w, group=128, out=None):
     _need(q, torch.uint8, (N, K // 2), "q")
     _need(s, torch.float16, (N, K // group), "scales")
     _need(z, torch.uint8, (N, K // group), "zeros")
-    _check(lib().int4g_asym_quantize(_ptr(w), N, K, group, _ptr(q), _ptr(s), _ptr(z), _stream(w)))
+    _launch(w.get_device(), lib().int4g_asym_quantize, _ptr(w), N, K, group, _ptr(q), _ptr(s), _ptr(z))
     return q, s, z
 
 
@@ -471,8 +485,8 @@ def int4g_asym_gemv(x, q, scales, zeros, group=128, algo=ALGO_AUTO, out=None):
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     _need(out, torch.bfloat16, (M, N), "out")
-    _check(lib().int4g_asym_gemv_ex(_ptr(x), _ptr(q), _ptr(scales), _ptr(zeros), _ptr(out), M, N, K, group, algo,
-                                    _stream(x)))
+    _launch(x.get_device(), lib().int4g_asym_gemv_ex, _ptr(x), _ptr(q), _ptr(scales), _ptr(zeros), _ptr(out), M, N, K,
+            group, algo)
     return out
 
 
@@ -590,11 +604,6 @@ def _like(t, tokens, heads, d, stride):
     return _torch().empty_like(t) if stride == heads * d and t.is_contiguous() else t.new_empty((tokens, heads, d))
 
 
-def _raw_stream(index):
-    """The current stream of device `index` as an integer handle."""
-    return _torch()._C._cuda_getCurrentRawStream(index)
-
-
 def nvfp4_kv_write(k, v, cache, slots):
     """Quantize k, v (bf16 [tokens, heads, D]; token strides of a packed
     projection are fine) into the cache at `slots` (int64 [tokens]; negative:
@@ -606,7 +615,7 @@ def nvfp4_kv_write(k, v, cache, slots):
     if v_tokens != tokens:
         raise ValueError(f"v has {v_tokens} tokens, k has {tokens}")
     sp = _data(slots, _torch().int64, (tokens,), "slots", index)
-    _check(lib().nvfp4_kv_write(cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, sp, tokens, _raw_stream(index)))
+    _launch(index, lib().nvfp4_kv_write, cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, sp, tokens)
 
 
 def nvfp4_kv_read(cache, slots, out=None):
@@ -626,7 +635,7 @@ def nvfp4_kv_read(cache, slots, out=None):
         k, v = out
         _data(k, torch.bfloat16, shape, "k", index)
         _data(v, torch.bfloat16, shape, "v", index)
-    _check(lib().nvfp4_kv_read(cache._ref, sp, shape[0], k.data_ptr(), v.data_ptr(), _raw_stream(index)))
+    _launch(index, lib().nvfp4_kv_read, cache._ref, sp, shape[0], k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -680,9 +689,8 @@ def nvfp4_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, i
         kn, _, kos = _rows(ko, hk, d, "out k", index)
         if qn != tokens or kn != tokens:
             raise ValueError(f"out must hold {tokens} tokens")
-    _check(lib().nvfp4_qk_norm_rope(q.data_ptr(), qs, qw, qo.data_ptr(), qos, hq, k.data_ptr(), ks, kw, ko.data_ptr(),
-                                    kos, hk, d, cp, max_pos, rot, 1 if interleaved else 0, pp, eps, tokens,
-                                    _raw_stream(index)))
+    _launch(index, lib().nvfp4_qk_norm_rope, q.data_ptr(), qs, qw, qo.data_ptr(), qos, hq, k.data_ptr(), ks, kw,
+            ko.data_ptr(), kos, hk, d, cp, max_pos, rot, 1 if interleaved else 0, pp, eps, tokens)
     return qo, ko
 
 
@@ -706,9 +714,8 @@ def nvfp4_qk_norm_rope_write(q, k, v, q_weight, k_weight, cos_sin, positions, ca
         n, _, stride = _rows(out, hq, d, "out", index)
         if n != tokens:
             raise ValueError(f"out must hold {tokens} tokens")
-    _check(lib().nvfp4_qk_norm_rope_write(cache._ref, q.data_ptr(), qs, qw, out.data_ptr(), stride, hq, k.data_ptr(), ks,
-                                          kw, v.data_ptr(), vs, cp, max_pos, rot, 1 if interleaved else 0, pp, eps, sp,
-                                          tokens, _raw_stream(index)))
+    _launch(index, lib().nvfp4_qk_norm_rope_write, cache._ref, q.data_ptr(), qs, qw, out.data_ptr(), stride, hq,
+            k.data_ptr(), ks, kw, v.data_ptr(), vs, cp, max_pos, rot, 1 if interleaved else 0, pp, eps, sp, tokens)
     return out
 
 
@@ -769,7 +776,7 @@ def nvfp4_kv_attention(q, cache, page_table, kv_lens, q_starts=None, max_q_len=N
             wp = workspace.data_ptr()
     else:
         wp, wn = _data(workspace, torch.uint8, None, "workspace", index), workspace.numel()
-    _check(lib().nvfp4_kv_attention(cache._ref, q.data_ptr(), qs, hq, starts, batch, total, max_q_len, tp, width, lens,
-                                    max_kv_len, prefix, prefix_len, d ** -0.5 if scale is None else scale,
-                                    out.data_ptr(), wp, wn, _raw_stream(index)))
+    _launch(index, lib().nvfp4_kv_attention, cache._ref, q.data_ptr(), qs, hq, starts, batch, total, max_q_len, tp,
+            width, lens, max_kv_len, prefix, prefix_len, d ** -0.5 if scale is None else scale, out.data_ptr(), wp,
+            wn)
     return out

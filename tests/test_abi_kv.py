@@ -268,3 +268,45 @@ def test_stride_of_a_single_token_does_not_matter():
     assert q._rows(one, 2, 128, "k", -1) == (1, 2, 256)
     assert q._rows(one[:0], 2, 128, "k", -1) == (0, 2, 256)
     assert q._rows(torch.as_strided(buf, (2, 2, 128), (300, 128, 1)), 2, 128, "k", -1) == (2, 2, 300)
+
+
+def test_launches_run_with_the_operands_device_current(monkeypatch):
+    """A null stream is the current device's: a call on another device's
+    tensors makes that device current for the launch, and only for it."""
+    import torch
+    q.lib()
+    now = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    seen = []
+
+    def entry(*args):
+        seen.append((now[0],) + args)
+        return status
+
+    status = OK
+    for index in (0, 3):
+        q._launch(index, entry, "a", 7)
+        assert seen.pop() == (index, "a", 7, 100 + index) and now == [0]
+    status = SHAPE
+    with pytest.raises(q.Nvfp4Error):
+        q._launch(3, entry)
+    assert now == [0]
+    # every function of the binding goes that way
+    import inspect
+    source = inspect.getsource(q)
+    for name in q.SIGNATURES:
+        if f"lib().{name}(" in source:
+            assert name.endswith(("_bytes", "_slots", "last_error")), name
