@@ -58,7 +58,7 @@ __device__ __forceinline__ void write_k_block(const KvCache& c, int64_t slot, in
   const SlotPlace p = place_of(slot, c);
   const int64_t row = ((p.page * c.heads + head) << c.ps_log2) + p.at;
   uint32_t sc;
-  const uint2 codes = absmax_block(w, g, rg, sc);
+  const uint2 codes = absmax_block<true>(w, g, rg, sc);
   *reinterpret_cast<uint2*>(c.k_codes + row * (c.head_dim >> 1) + blk * 8) = codes;
   c.k_scales[row * (c.head_dim >> 4) + blk] = (uint8_t)sc;
 }
@@ -72,7 +72,7 @@ __device__ __forceinline__ void write_v_block(const KvCache& c, int64_t slot, in
   const int64_t frag = ((p.page * c.heads + head) << (c.ps_log2 - 4)) + (p.at >> 4);
   const int tok = p.at & 15;
   uint32_t sc;
-  const uint2 codes = absmax_block(w, g, rg, sc);
+  const uint2 codes = absmax_block<true>(w, g, rg, sc);
   uint8_t* dst = c.v_codes + frag * (c.head_dim * 8) + blk * 128 + tok;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -20,11 +20,14 @@ namespace nvfp4k {
 // included) and no separate sign step.  It equals the division for every
 // bf16 significand, of either sign, against every fp32 significand
 // (tests/quotient_check.c runs all 2^30 pairs) as long as no step under- or
-// overflows, which holds for 2^-64 <= d < 2^100; blocks outside that range
-// divide.
+// overflows, which holds for finite x and 2^-64 <= d < 2^100; blocks outside
+// that range, or with an infinity or NaN, divide (of an infinity the
+// remainder is NaN, and the sign lost).
 constexpr float kQuotLo = 0x1p-64f, kQuotHi = 0x1p100f;
 
 __device__ __forceinline__ bool quot_fast(float d) { return d >= kQuotLo && d < kQuotHi; }
+// The same for a block whose largest bf16 magnitude pattern is amax_bits.
+__device__ __forceinline__ bool quot_fast(float d, uint32_t amax_bits) { return quot_fast(d) && amax_bits < 0x7F80u; }
 
 // |x| / d (one rounding: the element step above) carrying the sign of x,
 // for x given as the fp32 pattern of a bf16 value.
@@ -103,14 +106,17 @@ __device__ __forceinline__ uint32_t scale_code(float amax_b, float top, float g,
 
 // Scale byte and codes of the block of 16 bf16 values in w (element 2 i in
 // the low and 2 i + 1 in the high half of w[i]) under the absmax rule and
-// global scale g (rg = scale_recip(g)).
+// global scale g (rg = scale_recip(g)).  kGiven: g is any given scale, not
+// the tensor's amax / 2688 (with which a block that holds an infinity or NaN
+// has an infinite or NaN d, and divides in any case).
+template <bool kGiven = false>
 __device__ __forceinline__ uint2 absmax_block(const uint32_t (&w)[8], float g, float rg, uint32_t& sc) {
   uint32_t amax_bits = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax_bits = max(amax_bits, bf16x2_absmax_bits(w[i]));
   sc = scale_code(bf16_bits_to_f32(amax_bits), 6.0f, g, rg);
   const float d = e4m3_to_f32(sc) * g;
-  return quot_fast(d) ? encode_block<true>(w, d, 1.0f / d) : encode_block<false>(w, d, 0.0f);
+  return quot_fast(d, kGiven ? amax_bits : 0u) ? encode_block<true>(w, d, 1.0f / d) : encode_block<false>(w, d, 0.0f);
 }
 
 }  // namespace nvfp4k

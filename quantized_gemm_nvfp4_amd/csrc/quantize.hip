@@ -141,7 +141,7 @@ __device__ __forceinline__ void quantize_block_words(const uint4 v0, const uint4
     }
   }
   const float d = e4m3_to_f32(sc) * g;
-  codes[b] = quot_fast(d) ? encode_block<true>(w, d, 1.0f / d) : encode_block<false>(w, d, 0.0f);
+  codes[b] = quot_fast(d, amax_bits) ? encode_block<true>(w, d, 1.0f / d) : encode_block<false>(w, d, 0.0f);
   scales[b] = (uint8_t)sc;
 }
 

@@ -284,3 +284,25 @@ def test_norm_of_rows_whose_squares_are_denormal(sigma, eps):
     torch.cuda.synchronize()
     check_norm(host_bits(yq), bits.reshape(20, 4, 128)[:, :3], None, table, pos, eps, 128, False)
     check_norm(host_bits(yk), bits.reshape(20, 4, 128)[:, 3:], None, table, pos, eps, 128, False)
+
+
+def test_infinities_keep_their_sign():
+    """code = sign(x) | E2M1(|x| / d) holds for infinities too, under a given
+    global scale, in nvfp4_quantize and in the write."""
+    torch = need_gpu()
+    import quantized_gemm_nvfp4_amd as q
+    log("infinities under a given scale")
+    h, d = 2, 64
+    bits = workloads.random_bf16(821, (5, h * d))
+    for t, at, x in ((0, 3, np.inf), (1, 20, -np.inf), (2, 64, -np.inf), (2, 67, np.inf), (4, 127, -np.inf)):
+        bits[t, at] = F.bf16_bits(np.array([x], np.float32))[0]
+    for g in (KG, 2.0 ** -70):                           # quotients from reciprocals, and divided
+        wc, ws = KV.quantize_rows(bits.reshape(5, h, d), np.float32(g))
+        c, s, _ = q.nvfp4_quantize(dev_bf16(bits).view(5 * h, d), global_scale=torch.full((1,), g, device="cuda"))
+        cache = q.nvfp4_kv_cache(1, 16, h, d, g, g)
+        q.nvfp4_kv_write(dev_bf16(bits).view(5, h, d), dev_bf16(bits).view(5, h, d), cache, torch.arange(5, device="cuda"))
+        torch.cuda.synchronize()
+        assert np.array_equal(host_u8(c).reshape(wc.shape), wc) and np.array_equal(host_u8(s).reshape(ws.shape), ws)
+        for pages, want, frag in ((cache.k_codes, wc, False), (cache.k_scales, ws, False),
+                                  (cache.v_codes, wc, True), (cache.v_scales, ws, True)):
+            assert np.array_equal(np.stack([KV.rows_at(host_u8(pages), t, frag) for t in range(5)]), want)
