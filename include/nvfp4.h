@@ -457,7 +457,12 @@ typedef struct nvfp4_kv_cache {
  * so views of a packed projection serve as they are).  slots: int64
  * [tokens]; a token whose slot is padding is skipped.  Two tokens with the
  * same slot race.  Codes and scales are those of nvfp4_quantize with the
- * cache's global scale.
+ * cache's global scale.  What is stored is always finite: a block that holds
+ * an infinity or a NaN gets the largest scale, 448; these values become
+ * 6 * 448 * gscale with their sign bit, and the block's other values are
+ * rounded to that coarse grid, so an infinity or a NaN in K or V does not
+ * show as one later on.  A query that does not see the token is not touched
+ * by it, where a NaN in V would reach it through a weight of zero.
  */
 nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const void* k_bf16, int64_t k_stride,
                             const void* v_bf16, int64_t v_stride, const int64_t* slots,
@@ -497,7 +502,9 @@ nvfp4_status nvfp4_qk_norm_rope(const void* q_bf16, int64_t q_stride, const void
 /*
  * nvfp4_qk_norm_rope with the normed and rotated K, and V, going straight to
  * the cache: one launch, the same q_out and cache bytes as
- * nvfp4_qk_norm_rope followed by nvfp4_kv_write.
+ * nvfp4_qk_norm_rope followed by nvfp4_kv_write.  So where a position lies
+ * outside the table, q_out is NaN but the cache holds finite values (see
+ * nvfp4_kv_write).
  */
 nvfp4_status nvfp4_qk_norm_rope_write(const nvfp4_kv_cache* cache, const void* q_bf16,
                                       int64_t q_stride, const void* q_weight_bf16, void* q_out_bf16,

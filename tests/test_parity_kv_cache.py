@@ -306,3 +306,63 @@ def test_infinities_keep_their_sign():
         for pages, want, frag in ((cache.k_codes, wc, False), (cache.k_scales, ws, False),
                                   (cache.v_codes, wc, True), (cache.v_scales, ws, True)):
             assert np.array_equal(np.stack([KV.rows_at(host_u8(pages), t, frag) for t in range(5)]), want)
+
+
+def test_infinities_and_nan_are_stored_finite():
+    """As nvfp4_quantize stores them, in every form of the write; and a query
+    that does not see such a token has the same output as without it."""
+    torch = need_gpu()
+    import quantized_gemm_nvfp4_amd as q
+    log("infinities and NaN into the cache")
+    tokens, h, d = 40, 2, 128
+    k = dev_bf16(workloads.random_bf16(811, (tokens, h * d))).view(tokens, h, d)
+    v = dev_bf16(workloads.random_bf16(812, (tokens, h * d))).view(tokens, h, d)
+    bad_k, bad_v = k.clone(), v.clone()
+    for t, x in ((30, float("nan")), (31, float("inf")), (32, -float("inf")), (33, -float("nan"))):
+        bad_k[t, 0, t] = bad_v[t, 1, 2 * t] = x
+    slots = torch.arange(tokens, device="cuda") + 5
+    caches = []
+    for a, b in ((k, v), (bad_k, bad_v)):
+        c = make_cache(torch, q, 3, 16, h, d)
+        q.nvfp4_kv_write(a, b, c, slots)
+        caches.append(c)
+    clean, bad = caches
+    back = q.nvfp4_kv_read(bad, slots)
+    for rows, g, got, pages, frag in ((bad_k, bad.k_gscale, back[0], (bad.k_codes, bad.k_scales), False),
+                                      (bad_v, bad.v_gscale, back[1], (bad.v_codes, bad.v_scales), True)):
+        codes, scales, _ = q.nvfp4_quantize(rows.view(tokens * h, d), global_scale=g)
+        for want, have in zip((codes, scales), pages):
+            plain = np.stack([KV.rows_at(host_u8(have), s, frag) for s in slots.tolist()])
+            assert np.array_equal(plain, host_u8(want).reshape(plain.shape))
+        assert torch.isfinite(got.float()).all()
+        odd = ~torch.isfinite(rows)
+        top = torch.full_like(got.float(), 1.0) * 6 * 448 * g
+        assert torch.equal(got[odd].float().abs(), top.bfloat16()[odd].float())
+        keep = odd & ~torch.isnan(rows)
+        assert torch.equal(got[keep] > 0, rows[keep] > 0)
+    # queries 0 .. 39 of one sequence whose keys are all 40 tokens: 0 .. 29 see none of the four
+    table = torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([tokens + 5], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, tokens], dtype=torch.int32, device="cuda")
+    first = torch.arange(5, device="cuda")                              # the slots in front
+    for c in caches:
+        q.nvfp4_kv_write(k[:5], v[:5], c, first)
+    qs = dev_bf16(workloads.random_bf16(813, (tokens, 8 * d))).view(tokens, 8, d)
+    a, b = (q.nvfp4_kv_attention(qs, c, table, lens, q_starts=starts, max_q_len=tokens) for c in caches)
+    torch.cuda.synchronize()
+    assert torch.equal(a[:30].view(torch.int16), b[:30].view(torch.int16)) and torch.isfinite(b.float()).all()
+
+    # a position outside the table, in the one-launch form
+    cos_sin = torch.cat((torch.ones(10, 64), torch.zeros(10, 64)), 1).cuda()
+    pos = torch.tensor([3, 10, -1, 9], dtype=torch.int32, device="cuda")
+    one, two = make_cache(torch, q, 1, 16, h, d), make_cache(torch, q, 1, 16, h, d)
+    st = torch.arange(4, device="cuda")
+    yq = q.nvfp4_qk_norm_rope_write(qs[:4], k[:4], v[:4], None, None, cos_sin, pos, one, st)
+    _, yk = q.nvfp4_qk_norm_rope(qs[:4], k[:4], None, None, cos_sin, pos)
+    q.nvfp4_kv_write(yk, v[:4], two, st)
+    rk, rv = q.nvfp4_kv_read(one, st)
+    torch.cuda.synchronize()
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(one, name), getattr(two, name)), name
+    nan = torch.isnan(yq).flatten(1).any(1).tolist()
+    assert nan == [False, True, True, False] and torch.isfinite(rk.float()).all() and torch.isfinite(rv.float()).all()
