@@ -1466,7 +1466,15 @@ KvAttention without_keys(const KvCache& c, const KvAttention& a) {
 bool kv_attention_supported(const KvCache& c, const KvAttention& a) {
   const Plan p = make_plan(c, without_keys(c, a));
   const int64_t all = (int64_t)a.batch * c.heads * p.cut.own_tiles * std::max<int64_t>(1, ceil_div(a.max_kv_len, kPass));
-  return all <= (INT32_MAX >> 1) && p.prefix_items + p.own_items <= INT32_MAX;
+  // a grid holds fewer than 2^32 threads
+  auto fits = [](int64_t groups, int threads) { return groups * threads <= (int64_t)UINT32_MAX; };
+  const int tile_threads = c.head_dim == 64    ? Tile<64>::kThreads
+                           : c.head_dim == 128 ? Tile<128>::kThreads
+                                               : Tile<256>::kThreads;
+  auto threads = [&](int mt) { return mt > 0 ? 256 : tile_threads; };
+  const bool one_launch = p.prefix_items == 0 || p.prefix_mt == p.own_mt;
+  return all <= (INT32_MAX >> 1) && fits(p.own_items + (one_launch ? p.prefix_items : 0), threads(p.own_mt)) &&
+         fits(p.prefix_items, threads(p.prefix_mt)) && (p.parts == 0 || fits(ceil_div(a.total_q * a.q_heads, 4), 256));
 }
 
 int64_t kv_attention_workspace_bytes(const KvCache& c, const KvAttention& a) {

@@ -310,3 +310,18 @@ def test_launches_run_with_the_operands_device_current(monkeypatch):
     for name in q.SIGNATURES:
         if f"lib().{name}(" in source:
             assert name.endswith(("_bytes", "_slots", "last_error")), name
+
+
+def test_calls_past_a_grid_are_refused_before_anything_runs():
+    """A grid holds fewer than 2^32 threads: 64 a row for the join, 256 or 512
+    for a segment."""
+    f = q.lib().nvfp4_kv_attention_workspace_bytes
+    one = cache(heads=1, d=64)
+    rows = 1 << 20
+    assert f(one, 63, rows, rows, 1, 16, 16) > 0
+    big = dict(c=one, qs=64 * 64, hq=64, batch=rows, total=rows, table=T, width=1, mkv=16, pre=SL, plen=16)
+    assert f(one, 64, rows, rows, 1, 16, 16) == 0
+    assert att(**big) == UNSUP and "too large" in err()
+    # segments: 2^24 workgroups of 256 threads, without partial results
+    many = cache(heads=16, d=64)
+    assert att(c=many, qs=16 * 64, hq=16, batch=rows, total=rows, width=1, mkv=16) == UNSUP and "too large" in err()
