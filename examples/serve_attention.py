@@ -100,7 +100,7 @@ class Server:
                           q_starts=torch.tensor([0, t1 - t0], dtype=torch.int32, device="cuda"),
                           max_q_len=t1 - t0, max_kv_len=t1)
             out.append(h)
-        return torch.cat(out)
+        return torch.cat(out) if out else x
 
     def fill_prompts(self, x, lengths):
         """All sequences' prompts, packed in x [sum of lengths, hidden]."""
@@ -111,6 +111,8 @@ class Server:
         self.lens.copy_(torch.tensor(lengths, dtype=torch.int32))
         h = x
         for layer in self.layers:
+            if self.prefix == 0:
+                layer.calibrate(h)
             h = layer(h, self.table, at + self.prefix, slots, page_table=self.page_table, kv_lens=self.lens,
                       q_starts=starts, max_q_len=max(lengths), max_kv_len=max(lengths), prefix_pages=self.prefix_pages,
                       prefix_len=self.prefix)

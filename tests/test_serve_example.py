@@ -62,3 +62,12 @@ def test_main_prints_a_rate(capsys):
                     "3", "--prefix", "100", "--chunk", "64", "--prompt", "20", "--steps", "3", "--check"])
     out = capsys.readouterr().out
     assert "ms a step" in out and "relative error" in out
+
+
+def test_main_without_a_prefix(capsys):
+    need_gpu()
+    log("serving example without a shared prefix")
+    example().main(["--layers", "2", "--hidden", "512", "--q-heads", "4", "--kv-heads", "2", "--head-dim", "128", "--batch",
+                    "1", "--prefix", "0", "--prompt", "20", "--steps", "3", "--check"])
+    out = capsys.readouterr().out
+    assert "ms a step" in out and "relative error" in out
