@@ -483,7 +483,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, in
  *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s)   for the pairs of the first
  * rot_dim values, (i, i + rot_dim/2) or, interleaved, (2i, 2i + 1), with c
  * and s entries i and rot_dim/2 + i of row positions[token] of cos_sin
- * (fp32 [max_pos, rot_dim]).  Everything in fp32, rounded once to bf16.
+ * (fp32 [max_pos, rot_dim]).  Everything in fp32, rounded once to bf16 (a row
+ * whose sum of squares passes fp32's range gives zeros).
  * q: bf16 [tokens, q_heads, head_dim], q_stride values between tokens (a
  * multiple of 8); k likewise with k_heads.  Weights: bf16 [head_dim] or NULL
  * (no weight).  rot_dim: a multiple of 8 up to head_dim (0: norm only;
@@ -538,10 +539,10 @@ nvfp4_status nvfp4_qk_norm_rope_write(const nvfp4_kv_cache* cache, const void* q
  * them.  max_kv_len: an upper bound of kv_lens known to the host, at most
  * table_width * page_size; it sizes the launch.  page_table: int32 [batch,
  * table_width].  prefix_pages: int32 [ceil(prefix_len / page_size)].
- * scale: positive and finite.
+ * scale: positive, at most 1e30.
  * Numerics: q is taken in fp16 after an exact power-of-two scaling per row
- * (values below 2^-38 of the row's largest are flushed), K and V decode to
- * fp16 exactly, scores, softmax statistics and sums are fp32, and the softmax
+ * (exact down to 2^-31 of the row's largest value, rounded below that, flushed
+ * below 2^-38), K and V decode to fp16 exactly, scores, softmax statistics and sums are fp32, and the softmax
  * weights are rounded to fp16 for the product with V (11 bits; a weight below
  * 2^-32 of the row's largest may be lost).  Results do not depend on the order
  * in which workgroups run; how the keys are cut, and with it the last bits,

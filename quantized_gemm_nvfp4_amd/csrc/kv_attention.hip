@@ -203,10 +203,9 @@ __device__ __forceinline__ void own_rows_of(const KvAttention& a, int group, Ite
 //
 // Bound by HBM with one row tile.  64 query on 8 key heads of 128 over 48
 // sequences of 0 to 16000 keys, 488 MB: 102 us, 4.8 TB/s (a plain read reaches
-// 6.2); over one of 500009, 576 MB: 112 us, 5.1 TB/s.  The loop itself runs at
-// about 6.7 TB/s; the rest is the start, where lengths, pages and keys are
-// loaded one after the other (2 to 3 us, 7 to 9 while all workgroups do it),
-// and the uneven end.
+// 6.2); over one of 500009, 576 MB: 112 us, 5.1 TB/s.  What is lost is the
+// start, where lengths, pages and keys are loaded one after the other (2 to 3
+// us, 7 to 9 while all workgroups do it), and the uneven end.
 template <int D, int kTiles>
 struct Stream {
   static constexpr int kWaves = 4;
@@ -358,9 +357,10 @@ __global__ __launch_bounds__(256, (Stream<D, kTiles>::kOccupancy)) void kv_atten
       // Pages: of the fragments a lane takes K codes from (r / 4) and everything
       // else from (g).  Pages of 64 keys or more hold a whole pass of a wave: with
       // kWide one page number serves it and every address is a scalar base and a
-      // lane offset that never changes (single tokens on heads of 64 values: 36.5
-      // us, 37.8 the other way; 60 rows of 256 values 79.6 and 82.0; single
-      // tokens on heads of 128 alike).  A fragment past the segment's end takes
+      // lane offset that never changes (48 single tokens, 12 on 4 heads of 64
+      // values: 34.9 us, 36.2 the other way; 16 sequences of 32 rows of 128 values
+      // 42.2 and 43.0; single tokens on heads of 128 and 60 rows of 256 alike).
+      // A fragment past the segment's end takes
       // its last key's page, one outside the pool page 0 (masked).  Page numbers
       // are carried as they are in memory, so that a load in flight is first
       // waited for where it is used (a scalar load would be waited for by the
@@ -713,8 +713,8 @@ __global__ __launch_bounds__(256, (Stream<D, kTiles>::kOccupancy)) void kv_atten
 // large fp16 library product reaches 1157.  Decoding in the phases between the products, not beside them,
 // took 876 us; all waves in one phase at a time, 936; without the tiles in LDS,
 // each wave decoding for itself, 1570.  With 64 values the softmax, which costs
-// the same for a key, weighs twice as much: 763 TFLOP/s; with 256 one wave a
-// SIMD is left and nothing runs under its softmax: 789.
+// the same for a key, weighs twice as much: 763 TFLOP/s; with 256 the sums leave
+// one wave a SIMD, whose softmax stands between its products: 789.
 template <int D>
 struct Tile {
   // rows a workgroup takes: 8 waves of 32 with two waves to a SIMD, so that one
@@ -1307,16 +1307,21 @@ int tile_rows(int d) { return d == 64 ? Tile<64>::kRows : d == 128 ? Tile<128>::
 //   One while all passes of all tiles are at most eight for every compute unit:
 //   the call waits for latencies then, and more workgroups beat fewer reads (24
 //   rows of 256 values, 4 heads: 12.7 against 24.5 us with two tiles at 1503
-//   keys, 21 against 32 at 20000, but 66 against 57 at 16 x 10000 keys) and beat
+//   keys, 21 against 32 at 20000, but 74 against 61 at 16 x 4000 to 16000) and beat
 //   the tile kernel (4 heads of 128 values: 256 rows x 3000 keys 15 against 30
 //   us, 2048 x 600 15 against 25, 512 x 3000 24 against 27; past the limit 1024
 //   x 3000 32 and 32, 256 x 20000 37 against 34).
 //   Otherwise two, while they cost less than the tile kernel, which takes the
 //   same time for each of its tiles whether full or not: that of 5.75 pairs of
-//   row tiles (of 3.5 with 256 values, where it has 128 rows for 256).  24
-//   sequences of 8000 to 16000 keys, 8 heads of 128: 96 rows 177 against 315
-//   us, 128 rows 226 against 318, 192 rows 332 against 316; 4 such sequences:
-//   160 rows 61 against 71, 256 rows 84 against 73, 288 rows 91 against 114.
+//   row tiles (of 3.5 with 256 values, where it has 128 rows for 256).
+//   Sequences of 8000 to 16000 keys, every one with this many rows a head, in
+//   us, two row tiles against the tile kernel:
+//                           rows  32      96      128     160     192     256     288
+//     24 on 8 heads of  64   61/255 141/262 173/259 221/264 252/272 318/279 372/495
+//     24 on 8 heads of 128   90/326 229/346 272/354 355/364 391/373 494/392 590/658
+//     4 on 8 heads of 128    31/68   51/74   61/76   71/78   80/80  102/84  111/129
+//     24 on 4 heads of 256   95/273 232/290 279/296 372/527 404/523 581/533 617/848
+//   (64 values at 192 rows and 256 at 128 would do a few percent better the other way).
 int stream_tiles(int64_t rows, int d, int64_t passes) {
   if (rows <= 16 || passes * ceil_div(rows, 16) <= 8 * device_cus()) return 1;
   return 4 * ceil_div(rows, 32) < (d < 256 ? 23 : 14) * ceil_div(rows, tile_rows(d)) ? 2 : 0;
@@ -1334,9 +1339,12 @@ int stream_workers(int d, int mt) {
 // card (a workgroup a compute unit) and the keys a workgroup takes, of which its
 // start and end and its share of the join cost some 512: one round of 2048 keys
 // takes 108 us and two of half that 126 (512 rows x 8 heads x 32728 keys), but
-// 24 x 8 tiles in four chunks, three full rounds, 324 against 374 in a round
-// three quarters full.  None shorter than 256 keys (512: 36 against 32 us for 1024 rows x 4
-// heads x 3000 keys).
+// 24 x 8 tiles of 64 values in four chunks, three full rounds, 283 against 305 in
+// a round three quarters full, 24 x 4 of 256 values 296 against 343 (of 128
+// values both 392).  With 64, 128 and 256 values anything from 256 to 2048 in
+// the place of 512 measures alike; 64 cuts too finely (256 rows x 8 heads x
+// 30000 keys of 64 values: 189 us, 167).  None shorter than 256 keys (512: 36
+// against 32 us for 1024 rows x 4 heads x 3000 keys).
 void cut_tiles(int64_t keys, int64_t base, int& chunks, int& chunk) {
   const int64_t cus = device_cus(), most = std::max<int64_t>(1, keys / 256);
   int64_t want = 1, least = INT64_MAX;
@@ -1443,9 +1451,10 @@ void run_attention(const KvCache& c, const KvAttention& a, const Plan& p, hipStr
   if (p.parts == 0) return;
   // one wave a row, or four where few rows may have more parts than a wave loads
   // at once: 64 rows of 96 parts of 128 values take 125 against 133 us for the
-  // call, 96 rows of 7 parts of 256 values 12.4 against 13.0, but 32 rows of 5
-  // parts of 128 values 10.3 against 10.0, and 4096 rows of 18 parts 12.0
-  // against 8.3 us in this kernel
+  // call, 96 rows of 7 parts of 256 values 12.4 against 13.0, 32 of 79 parts of
+  // 64 values 13.0 against 14.7, but 32 rows of 5 parts of 128 values 10.3
+  // against 10.0, 32 of 16 parts of 64 values 9.4 against 9.3, and 4096 rows of
+  // 18 parts 12.0 against 8.3 us in this kernel
   const int64_t own_parts = std::max<int64_t>(p.cut.own_chunks, p.cut.workers / ((int64_t)a.batch * c.heads * p.cut.own_tiles) + 1);
   const int64_t rows = a.total_q * a.q_heads;
   if (rows >= 1024 || p.cut.prefix_chunks + own_parts <= 4 * (256 / D))
